@@ -423,10 +423,14 @@ def sf_attention_cached_workspace(eng, T, n, max_len, params):
 
 
 def _scratch(size, q, stream):
-    ws = torch.empty(size, dtype=torch.uint8, device=q.device)
-    if stream is not None:   # torch must not hand it on while another stream still uses it
-        ws.record_stream(torch.cuda.ExternalStream(stream, device=q.device))
-    return ws
+    """A workspace for one call on `stream` (None: torch's current one), from that stream's own pool: a block that
+    torch takes on one stream may still be in use there, and only that stream's order keeps the two uses apart."""
+    if stream is None:
+        return torch.empty(size, dtype=torch.uint8, device=q.device)
+    # 0 and 1 are CUDA's handles of the default stream
+    on = torch.cuda.default_stream(q.device) if stream in (0, 1) else torch.cuda.ExternalStream(stream, device=q.device)
+    with torch.cuda.stream(on):
+        return torch.empty(size, dtype=torch.uint8, device=q.device)
 
 
 # the calls of a single-frame step check and marshal their arguments natively (csrc/calls.cpp)
