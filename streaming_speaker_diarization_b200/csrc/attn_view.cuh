@@ -44,8 +44,9 @@ __host__ __device__ __forceinline__ void clamp_bounds(int rb, int re, int T, int
 __host__ __device__ __forceinline__ int64_t slot_base(const int* __restrict__ cu, int i, int mul, int per, int add) {
   return ((int64_t)cu[i] * mul >> per) + (int64_t)i * add;
 }
-constexpr int64_t MAX_SLOT = 1 << 22;   // slots of one sequence the kernels can index (x 256 rows stays in 32 bits)
-// wild offsets must not wrap: -1 (idle) .. 2^22 (past every sequence's work)
+// slots of one sequence the kernels can index: 2^26 rows in tiles of 8 (x 128 rows, the largest tile or page, stays in 32 bits)
+constexpr int64_t MAX_SLOT = 1 << 23;
+// wild offsets must not wrap: -1 (idle) .. 2^23 (past every sequence's work)
 __host__ __device__ __forceinline__ int slot_index(int64_t at) { return (int)(at < 0 ? -1 : at > MAX_SLOT ? MAX_SLOT : at); }
 // The sequence of a slot (the last whose base is at or before it), the slot's
 // index in it and its rows, by a whole warp: 32 bases are compared at once, one

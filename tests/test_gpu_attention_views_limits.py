@@ -1,0 +1,25 @@
+"""GPU: the limited-view attention at the ends of its documented ranges."""
+import numpy as np
+import pytest
+
+from test_gpu_attention_views import (b, cached_reference, check, engines, make_cache, make_table, np64, rows, run_cached,  # noqa: F401
+                                      torch)
+
+pytestmark = pytest.mark.gpu
+
+
+def test_one_sequence_of_more_rows_than_tiles_of_16_count(engines):  # noqa: F811
+    """2^25 + 128 rows x heads in one sequence, in 8-row tiles (fp32, heads of 128): every row is written.  All but the
+    last 64 new rows come out before position 0."""
+    H, KV, D, page, held = 8, 1, 128, 64, 64
+    T = 2 ** 22 + 16
+    table, pages = make_table(210, [held], page)
+    cache = make_cache(211, pages, KV, page, D)
+    q, out = (torch.zeros(T, H, D, device="cuda") for _ in range(2))
+    q[-held:] = rows(212, held, H, D, "f32")
+    out.fill_(7.0)
+    run_cached(engines["f32"], q, cache, table, [held], [T], dict(right=0), D, out=out)
+    b.sf_check(engines["f32"])
+    assert not out[:-held].any()
+    ref, spread, big = cached_reference(np64(q[-held:]), cache, table, [held], [held], dict(right=0), D, H)
+    check(np64(out[-held:]), ref, spread, big, "cached", "f32", D, "limits", 0)
