@@ -134,12 +134,11 @@ template <bool EXACT> __device__ __forceinline__ float tanh_of(float y, bool wid
 // / G, head r % G of the key/value head).
 struct RowTile {
   int s, sb, n_new, r0, rows;   // rows: 0 for an idle slot
-  bool bad;                     // offsets out of order or range
 };
 template <int R> __device__ __forceinline__ RowTile row_tile(const KvSeqs& q, int64_t slot, int G) {
   RowTile r;
   int tile, se;
-  r.s = slot_at(q.cu, q.n, q.T, slot, G, R == 8 ? 3 : 4, 1, tile, r.sb, se, r.bad);
+  r.s = slot_at(q.cu, q.n, q.T, slot, G, R == 8 ? 3 : 4, 1, tile, r.sb, se);
   r.n_new = se - r.sb;
   r.r0 = tile * R;
   r.rows = tile < 0 ? 0 : max(0, min(R, r.n_new * G - r.r0));
@@ -220,9 +219,12 @@ __global__ void __launch_bounds__(CW * 32, cached_ctas(sizeof(E) == 4, D, NQ))
   const int s = rt.s, sb = rt.sb, n_new = rt.n_new, r0 = rt.r0, rows = rt.rows;
   const int most = q.table_cols << page_log2;
   int held = q.held[s];
-  const bool bad = rt.bad || held < 0 || held > most;
+  const bool bad = held < 0 || held > most;
   held = min(max(held, 0), most);
-  if (bad && threadIdx.x == 0 && part == 0) set_err(err, ERR_BOUNDS);
+  if (threadIdx.x == 0 && part == 0) {
+    if (bad) set_err(err, ERR_BOUNDS);
+    if (kvh == 0) report_offsets(q.cu, blockIdx.x / parts, q.n, q.T, err);
+  }
   if (rows == 0) return;    // the whole cluster agrees
   // row r of the tile: new row tok(r), head kvh G + head(r); quotients below 2^11 by a rounded reciprocal
   const int tok0 = r0 / G, head0 = r0 - tok0 * G;

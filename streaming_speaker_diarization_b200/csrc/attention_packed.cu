@@ -52,7 +52,7 @@ struct PackedSmem {
 }  // namespace
 
 template <int D>
-__global__ void __launch_bounds__(256) attn_packed_f32_kernel(const __grid_constant__ PackedArgs<float> a,
+__global__ void __launch_bounds__(256, D == 64 ? 2 : 1) attn_packed_f32_kernel(const __grid_constant__ PackedArgs<float> a,
                                                                const __grid_constant__ AttnView w, int nc, int* err) {
   SF_PDL_ENTRY();
   extern __shared__ float ps_smem[];
@@ -66,9 +66,9 @@ __global__ void __launch_bounds__(256) attn_packed_f32_kernel(const __grid_const
   const int h = blockIdx.y, kvh = h / (a.n_heads / a.n_kv), rank = blockIdx.x % nc;
   int tile;
   int sb, se;
-  bool bad;
-  const int s = slot_at(a.cu, a.n, a.T, (gridDim.x - 1 - blockIdx.x) / nc, 1, 7, 1, tile, sb, se, bad);
-  if (bad && tid == 0) set_err(err, ERR_BOUNDS);
+  const unsigned slot = (gridDim.x - 1 - blockIdx.x) / nc;
+  const int s = slot_at(a.cu, a.n, a.T, slot, 1, 7, 1, tile, sb, se);
+  if (tid == 0 && h == 0) report_offsets(a.cu, slot, a.n, a.T, err);
   const int S = se - sb, i0 = tile * PR;
   if (tile < 0 || i0 >= S) return;   // the whole cluster agrees
   const int rows = min(PR, S - i0);

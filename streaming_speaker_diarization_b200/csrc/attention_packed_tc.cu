@@ -204,10 +204,8 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
   __shared__ int found[4];
   if (warp == 0) {
     int tile, sb, se;
-    bool bad;
-    const int s = slot_at(a.cu, a.n, a.T, slots - 1 - behind, 1, 7, 1, tile, sb, se, bad);
+    const int s = slot_at(a.cu, a.n, a.T, slots - 1 - behind, 1, 7, 1, tile, sb, se);
     if (lane == 0) {
-      if (bad) set_err(err, ERR_BOUNDS);
       found[0] = tile;
       found[1] = sb;
       found[2] = se - sb;
@@ -218,6 +216,8 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
                  "r"((uint32_t)L::TMEM)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else if (threadIdx.x == 96 && h == 0) {
+    report_offsets(a.cu, slots - 1 - behind, a.n, a.T, err);
   }
   tc_fence_before();
   __syncthreads();

@@ -30,11 +30,24 @@ __device__ __forceinline__ float capped_l2(float s, float cap) {
 
 // Rows [b, e) within [0, T) of a sequence with offsets rb and re: offsets are
 // read from device memory that the host has not seen, so each is clamped, and
-// bad reports an offset out of order or out of range.
+// bad says that an offset was out of order or out of range.
 __host__ __device__ __forceinline__ void clamp_bounds(int rb, int re, int T, int& b, int& e, bool& bad) {
   b = rb < 0 ? 0 : rb > T ? T : rb;
   e = re < b ? b : re > T ? T : re;
   bad = rb != b || re != e;
+}
+// Whether sequence i (if there is one) has such offsets.  Slot i of a call,
+// of which there are at least n, answers for sequence i: among offsets out of
+// order a sequence may own no slot.
+__host__ __device__ __forceinline__ bool bad_offsets(const int* __restrict__ cu, int64_t i, int n, int T) {
+  if (i < 0 || i >= n) return false;
+  int b, e;
+  bool bad;
+  clamp_bounds(cu[i], cu[i + 1], T, b, e, bad);
+  return bad;
+}
+__device__ __forceinline__ void report_offsets(const int* __restrict__ cu, int64_t slot, int n, int T, int* err) {
+  if (bad_offsets(cu, slot, n, T)) set_err(err, ERR_BOUNDS);
 }
 
 // Work slots over sequences whose lengths only the device knows: sequence i
@@ -54,7 +67,7 @@ __host__ __device__ __forceinline__ int slot_index(int64_t at) { return (int)(at
 // with the bounds, cost more in instructions than the loads: 64 windows 35.5
 // against 34.8 us).  Slots past a sequence's work are idle.
 __device__ __forceinline__ int slot_at(const int* __restrict__ cu, int n, int T, int64_t slot, int mul, int per, int add,
-                                       int& idx, int& b, int& e, bool& bad) {
+                                       int& idx, int& b, int& e) {
   const int lane = threadIdx.x & 31;
   int lo = 0, len = n;
   while (len > 1) {
@@ -65,6 +78,7 @@ __device__ __forceinline__ int slot_at(const int* __restrict__ cu, int n, int T,
     len = len - k * step < step ? len - k * step : step;
   }
   idx = slot_index(slot - slot_base(cu, lo, mul, per, add));
+  bool bad;
   clamp_bounds(cu[lo], cu[lo + 1], T, b, e, bad);
   return lo;
 }

@@ -95,16 +95,18 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const E* __restrict__ ki
   __shared__ uint32_t red[2][16];
   int nth;
   int sb, se;
-  bool bad;
-  const int s = slot_at(q.cu, q.n, q.T, blockIdx.x, 1, page_log2, 2, nth, sb, se, bad);
+  const int s = slot_at(q.cu, q.n, q.T, blockIdx.x, 1, page_log2, 2, nth, sb, se);
   const int held = max(q.held[s], -1), n_new = se - sb;   // (differences stay in 32 bits)
   int first = held - n_new;                    // position of the first new row
-  bad = bad || first < 0;
-  if (first < 0) {                             // rows before position 0 have no place
+  const bool bad = first < 0;
+  if (bad) {                                   // rows before position 0 have no place
     sb -= first;
     first = 0;
   }
-  if (bad && threadIdx.x == 0) set_err(err, ERR_BOUNDS);
+  if (threadIdx.x == 0) {
+    if (bad) set_err(err, ERR_BOUNDS);
+    if (blockIdx.y == 0) report_offsets(q.cu, blockIdx.x, q.n, q.T, err);
+  }
   if (nth < 0 || n_new <= 0 || held <= first) return;
   const int pi = (first >> page_log2) + nth;
   if ((int64_t)pi * c.page >= held) return;

@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from test_gpu_attention_views import (b, cached_reference, check, engines, make_cache, make_table, np64, rows, run_cached,  # noqa: F401
+from test_gpu_attention_views import (b, cached_reference, check, dev, engines, make_cache, make_table, np64, rows, run_cached,  # noqa: F401
                                       torch)
 
 pytestmark = pytest.mark.gpu
@@ -23,3 +23,22 @@ def test_one_sequence_of_more_rows_than_tiles_of_16_count(engines):  # noqa: F81
     assert not out[:-held].any()
     ref, spread, big = cached_reference(np64(q[-held:]), cache, table, [held], [held], dict(right=0), D, H)
     check(np64(out[-held:]), ref, spread, big, "cached", "f32", D, "limits", 0)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("cu", [[0, 200, 100, 300], [0, 90, 80, 300], [0, 200, 200, 190]])
+def test_offsets_out_of_order_are_reported(engines, dt, cu):  # noqa: F811
+    """Offsets that fall back, also where the sequence between them owns no slot: SF_EDEVICE, then all is well."""
+    KV, D, page, T, eng = 2, 64, 16, 300, engines[dt]
+    x, p = rows(220, T, KV, D, dt), b.attn_params(KV, KV, D)
+    cache, held = make_cache(221, 60, KV, page, D), dev([300, 300, 300])
+    table = dev(np.arange(60).reshape(3, 20))
+    calls = [lambda at: b.sf_attention_packed(eng, x, x, x, at, torch.empty_like(x), p),
+             lambda at: b.sf_kv_append(eng, x, x, at, held, table, cache),
+             lambda at: b.sf_attention_cached(eng, x, at, held, table, cache, torch.empty_like(x), p)]
+    for call in calls:
+        call(dev(cu))
+        with pytest.raises(b.SFError, match="SF_EDEVICE"):
+            b.sf_check(eng)
+        call(dev(sorted(cu)))
+        b.sf_check(eng)
