@@ -33,8 +33,9 @@
 // for a warp's rows: tanh(y) / y as a polynomial of degree 4 in y^2 (our own
 // fit at Chebyshev nodes, relative error 5.9e-7 on [0, 3/4]), with the score
 // factor, the cap and log2 e in its coefficients, so that the exponent is one
-// more multiply-add; otherwise 1 - 2 / (2^(2 y log2 e) + 1), whose absolute
-// error of 2.5e-7 is small against a score of that size.
+// more multiply-add; otherwise the polynomial or, for scores beyond its range,
+// 1 - 2 / (2^(2 y log2 e) + 1), whose absolute error of 2.5e-7 is small against
+// a score of that size.
 //
 // 0 x V of rows that do not see a key of their tile would carry an infinity or
 // NaN over: a row whose result is not finite although its sum is, and that sees
@@ -144,9 +145,17 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
   return (d & ~((uint64_t)0x3fff << 16)) | ((uint64_t)(TK * 128 >> 4) << 16);
 }
 
-constexpr float TANH_Y = 0.75f;   // range of the polynomial
-__device__ __forceinline__ float tanh_exp(float y) {
-  return 1.f - __fdividef(2.f, ex2_approx(y * (2.f * LOG2E)) + 1.f);
+// tanh(y) / y = sum c_k y^2k on |y| <= TANH_Y
+constexpr float TANH_Y = 0.75f;
+__device__ constexpr float TANH_C[5] = {9.99999463558197e-1f, -3.332834839820862e-1f, 1.3259831070899963e-1f,
+                                        -5.008019134402275e-2f, 1.2950727716088295e-2f};
+// tanh at any argument: the exponential's form has an absolute error, which is too much for a small one
+__device__ __forceinline__ float tanh_any(float y) {
+  const float u = y * y;
+  float p = TANH_C[4];
+#pragma unroll
+  for (int k = 3; k >= 0; --k) p = fmaf(p, u, TANH_C[k]);
+  return fabsf(y) <= TANH_Y ? p * y : 1.f - __fdividef(2.f, ex2_approx(y * (2.f * LOG2E)) + 1.f);
 }
 
 }  // namespace
@@ -373,9 +382,6 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
     // capped score in the log2 domain: s sum pc_k s^2k
     float pc[5];
     {
-      // tanh(y) / y = sum c_k y^2k on |y| <= 3/4
-      constexpr float TANH_C[5] = {9.99999463558197e-1f, -3.332834839820862e-1f, 1.3259831070899963e-1f,
-                                   -5.008019134402275e-2f, 1.2950727716088295e-2f};
       float y = w.cap * LOG2E * inv_cap;
 #pragma unroll
       for (int k = 0; k < 5; ++k) {
@@ -442,7 +448,7 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
               }
             } else {
 #pragma unroll
-              for (int c = 0; c < 32; ++c) sc[c] = f * tanh_exp(sc[c] * inv_cap);
+              for (int c = 0; c < 32; ++c) sc[c] = f * tanh_any(sc[c] * inv_cap);
             }
           } else {
 #pragma unroll
@@ -499,7 +505,7 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
               }
             }
           }
-          mx = near ? capped(make_float2(mx, mx), make_float2(0.f, 0.f)).x : f * tanh_exp(mx * inv_cap);
+          mx = near ? capped(make_float2(mx, mx), make_float2(0.f, 0.f)).x : f * tanh_any(mx * inv_cap);
         } else {
           mx *= f;
         }
@@ -571,7 +577,7 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
         weights([&](float2 v) { return capped(v, b2); });
       } else {
         weights([&](float2 v) {
-          return __ffma2_rn(make_float2(tanh_exp(v.x * inv_cap), tanh_exp(v.y * inv_cap)), f2, b2);
+          return __ffma2_rn(make_float2(tanh_any(v.x * inv_cap), tanh_any(v.y * inv_cap)), f2, b2);
         });
       }
       tmem_st_wait();
