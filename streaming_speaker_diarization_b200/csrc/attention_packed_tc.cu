@@ -33,7 +33,7 @@
 // for a warp's rows: tanh(y) / y as a polynomial of degree 4 in y^2 (our own
 // fit at Chebyshev nodes, relative error 5.9e-7 on [0, 3/4]), with the score
 // factor, the cap and log2 e in its coefficients, so that the exponent is one
-// more multiply-add; otherwise the polynomial or, for scores beyond its range,
+// more multiply-add; beyond, and for caps whose coefficients leave fp32's range, the polynomial or, for scores beyond its range,
 // 1 - 2 / (2^(2 y log2 e) + 1), whose absolute error of 2.5e-7 is small against
 // a score of that size.
 //
@@ -147,14 +147,30 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
 
 // tanh(y) / y = sum c_k y^2k on |y| <= TANH_Y
 constexpr float TANH_Y = 0.75f;
-__device__ constexpr float TANH_C[5] = {9.99999463558197e-1f, -3.332834839820862e-1f, 1.3259831070899963e-1f,
-                                        -5.008019134402275e-2f, 1.2950727716088295e-2f};
+constexpr float tanh_c(int k) {
+  constexpr float c[5] = {9.99999463558197e-1f, -3.332834839820862e-1f, 1.3259831070899963e-1f, -5.008019134402275e-2f,
+                          1.2950727716088295e-2f};
+  return c[k];
+}
+// coefficients of the capped score in the log2 domain, s sum pc_k s^2k for |s / cap| <= TANH_Y; false where their powers of
+// scale / cap leave fp32's range (caps far from the scores' size: at scale 1/8 below 1e-5 and above 1500) or there is no cap.
+// Judged on the host: by each thread from its own registers it cost tiles without a cap too (64 windows 34.7 against 32.1 us)
+__host__ __device__ __forceinline__ bool cap_coefficients(const AttnView& w, float* pc) {
+  const float inv_cap = w.cap > 0.f ? w.scale / w.cap : 0.f;
+  float y = w.cap * LOG2E * inv_cap;
+#pragma unroll
+  for (int k = 0; k < 5; ++k) {
+    pc[k] = tanh_c(k) * y;
+    y *= inv_cap * inv_cap;
+  }
+  return pc[4] > 1e-36f && pc[4] < 1e36f && pc[0] > 1e-36f && pc[0] < 1e36f;
+}
 // tanh at any argument: the exponential's form has an absolute error, which is too much for a small one
 __device__ __forceinline__ float tanh_any(float y) {
   const float u = y * y;
-  float p = TANH_C[4];
+  float p = tanh_c(4);
 #pragma unroll
-  for (int k = 3; k >= 0; --k) p = fmaf(p, u, TANH_C[k]);
+  for (int k = 3; k >= 0; --k) p = fmaf(p, u, tanh_c(k));
   return fabsf(y) <= TANH_Y ? p * y : 1.f - __fdividef(2.f, ex2_approx(y * (2.f * LOG2E)) + 1.f);
 }
 
@@ -164,7 +180,7 @@ template <int NG, int D>
 __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
     attn_packed_tc_kernel(const __grid_constant__ CUtensorMap t_q, const __grid_constant__ CUtensorMap t_k,
                           const __grid_constant__ CUtensorMap t_v, const __grid_constant__ PackedArgs<bf16> a,
-                          const __grid_constant__ AttnView w, int G, unsigned slots, int nc_log2, int* err) {
+                          const __grid_constant__ AttnView w, int poly, int G, unsigned slots, int nc_log2, int* err) {
   using L = PTc<NG, D>;
   extern __shared__ uint8_t pt_smem[];
   uint8_t* sm = pt_smem + ((1024 - (su32(pt_smem) & 1023)) & 1023);
@@ -379,16 +395,10 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
     const int hi = w.right < 0 ? S : min(S, i + w.right + 1);
     const float slope = w.slopes ? w.slopes[h] * LOG2E : 0.f;
     const float inv_cap = w.cap > 0.f ? w.scale / w.cap : 0.f;
-    // capped score in the log2 domain: s sum pc_k s^2k
+    const float f = w.cap > 0.f ? w.cap * LOG2E : w.scale * LOG2E;   // from s (tanh of it) to the log2 domain
+    const float2 f2 = make_float2(f, f);
     float pc[5];
-    {
-      float y = w.cap * LOG2E * inv_cap;
-#pragma unroll
-      for (int k = 0; k < 5; ++k) {
-        pc[k] = TANH_C[k] * y;
-        y *= inv_cap * inv_cap;
-      }
-    }
+    cap_coefficients(w, pc);
     auto capped = [&](float2 v, float2 add) {   // + add, for |s / cap| <= 3/4
       const float2 u = __fmul2_rn(v, v);
       float2 p = make_float2(pc[4], pc[4]);
@@ -397,6 +407,25 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
       p = __ffma2_rn(p, u, make_float2(pc[1], pc[1]));
       p = __ffma2_rn(p, u, make_float2(pc[0], pc[0]));
       return __ffma2_rn(p, v, add);
+    };
+    // columns x .. x + cols of the scores as they enter the exponent, in place, for any cap and score; the largest of them
+    // (rarely entered: a loop of its own, not unrolled)
+    auto cap_in_place = [&](int x, int cols) {
+      float top = -INFINITY;
+#pragma unroll 1
+      for (const int end = x + cols; x < end; x += 16) {
+        uint32_t v[16];
+        tmem_ld16(tm_s + x, v);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float y = f * tanh_any(__uint_as_float(v[c]) * inv_cap);
+          top = fmaxf(top, y);
+          v[c] = __float_as_uint(y);
+        }
+        tmem_st16(tm_s + x, v);
+      }
+      tmem_st_wait();
+      return top;
     };
     auto magnitude = [](const float* sc) {   // of 32
       float p0 = max3_abs(sc[0], sc[1], sc[2]), p1 = max3_abs(sc[3], sc[4], sc[5]);
@@ -407,8 +436,6 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
       }
       return max3_abs(max3_abs(p0, sc[30], sc[31]), p1, 0.f);
     };
-    const float f = w.cap > 0.f ? w.cap * LOG2E : w.scale * LOG2E;   // from s (tanh of it) to the log2 domain
-    const float2 f2 = make_float2(f, f);
     // first keys of the tiles that every row of the query tile sees whole: [w_lo, w_hi] by the window, up to w_pre
     const int w_lo = w.left < 0 ? 0 : r0 + TQ - 1 - w.left;
     const int w_hi = min(S, w.right < 0 ? S : r0 + w.right + 1) - TK, w_pre = pre - TK;
@@ -424,11 +451,11 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
       ++mine;
       tc_fence_after();
       const bool whole = (j0 >= w_lo && j0 <= w_hi) || j0 <= w_pre;
-      // First pass: the row's largest score, 32 columns at a time.  Scores that are masked or biased go back to TMEM as
-      // they enter the exponent; the others are taken as they are in the second pass.
+      // First pass: the row's largest score, 32 columns at a time.  Scores that are masked, biased or under a cap without
+      // coefficients go back to TMEM as they enter the exponent; the others are taken as they are in the second pass.
       // Of capped scores the largest magnitude does: it bounds them, and as a reference it is at most 2^(2 cap log2 e tanh
       // 3/4) above the largest weight (2^117 at cap 64, inside bf16's and fp32's range).
-      const bool ready = !whole || slope != 0.f;
+      const bool ready = !whole || slope != 0.f || (w.cap > 0.f && !poly);
       float mx = -INFINITY, mag = 0.f;
 #pragma unroll
       for (int x = 0; x < TK; x += 32) {
@@ -439,7 +466,7 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
         for (int c = 0; c < 32; ++c) sc[c] = __uint_as_float(v[c]);
         if (ready) {
           if (w.cap > 0.f) {
-            if (__all_sync(0xffffffffu, magnitude(sc) * inv_cap <= TANH_Y)) {
+            if (poly && __all_sync(0xffffffffu, magnitude(sc) * inv_cap <= TANH_Y)) {
 #pragma unroll
               for (int c = 0; c < 32; c += 2) {
                 const float2 y = capped(make_float2(sc[c], sc[c + 1]), make_float2(0.f, 0.f));
@@ -447,8 +474,10 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
                 sc[c + 1] = y.y;
               }
             } else {
+              cap_in_place(x, 32);
+              tmem_ld32(tm_s + x, v);
 #pragma unroll
-              for (int c = 0; c < 32; ++c) sc[c] = f * tanh_any(sc[c] * inv_cap);
+              for (int c = 0; c < 32; ++c) sc[c] = __uint_as_float(v[c]);
             }
           } else {
 #pragma unroll
@@ -490,24 +519,16 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
         }
       }
       const bool near = __all_sync(0xffffffffu, mag * inv_cap <= TANH_Y);   // capped scores in the polynomial's range
+      bool placed = ready;   // the scores stand in TMEM as they enter the exponent
       if (!ready) {
-        if (w.cap > 0.f) {
-          if (abs_ref) {
-            mx = mag;
-            if (!near) {   // a magnitude is no reference for scores this far out: the largest score itself
-              mx = -INFINITY;
-#pragma unroll
-              for (int x = 0; x < TK; x += 32) {
-                uint32_t v[32];
-                tmem_ld32(tm_s + x, v);
-#pragma unroll
-                for (int c = 0; c < 32; c += 2) mx = max3(mx, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-              }
-            }
-          }
-          mx = near ? capped(make_float2(mx, mx), make_float2(0.f, 0.f)).x : f * tanh_any(mx * inv_cap);
-        } else {
+        if (w.cap == 0.f) {
           mx *= f;
+        } else if (near) {
+          const float bound = abs_ref ? mag : mx;
+          mx = capped(make_float2(bound, bound), make_float2(0.f, 0.f)).x;
+        } else {   // a magnitude would be no reference for scores this far out
+          mx = cap_in_place(0, TK);
+          placed = true;
         }
       }
       // the reference of the tile before: this group's own, or handed on by the other
@@ -569,16 +590,12 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
           tmem_st16(tm_s + x / 2, pw);
         }
       };
-      if (ready) {
+      if (placed) {
         weights([&](float2 v) { return __fadd2_rn(v, b2); });
       } else if (w.cap == 0.f) {
         weights([&](float2 v) { return __ffma2_rn(v, f2, b2); });
-      } else if (near) {
-        weights([&](float2 v) { return capped(v, b2); });
       } else {
-        weights([&](float2 v) {
-          return __ffma2_rn(make_float2(tanh_any(v.x * inv_cap), tanh_any(v.y * inv_cap)), f2, b2);
-        });
+        weights([&](float2 v) { return capped(v, b2); });
       }
       tmem_st_wait();
       tc_fence_before();
@@ -744,7 +761,8 @@ cudaError_t launch_tc(const PackedArgs<bf16>& a, const AttnView& w, int64_t unit
   }
   cfg.attrs = attr;
   cfg.numAttrs = na;
-  CK_LAUNCH(cudaLaunchKernelEx(&cfg, attn_packed_tc_kernel<NG, D>, tq, tk, tv, a, w, a.n_heads / a.n_kv, (unsigned)(units / a.n_heads),
+  float pc[5];
+  CK_LAUNCH(cudaLaunchKernelEx(&cfg, attn_packed_tc_kernel<NG, D>, tq, tk, tv, a, w, (int)cap_coefficients(w, pc), a.n_heads / a.n_kv, (unsigned)(units / a.n_heads),
                                nc == 4 ? 2 : nc - 1, err));
   return cudaGetLastError();
 }
