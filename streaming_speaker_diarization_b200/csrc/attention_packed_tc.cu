@@ -53,6 +53,7 @@ namespace {
 constexpr int TQ = 128;   // rows of a query tile
 constexpr int TK = 64;    // keys of a tile
 constexpr float LAZY = 8.f;   // log2 of the largest weight before the reference maximum moves
+constexpr float FAR = 40.f;   // log2 of how far a magnitude may stand above a row's largest score as its reference
 
 template <int NG, int D>
 struct PTc {
@@ -439,7 +440,6 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
     // first keys of the tiles that every row of the query tile sees whole: [w_lo, w_hi] by the window, up to w_pre
     const int w_lo = w.left < 0 ? 0 : r0 + TQ - 1 - w.left;
     const int w_hi = min(S, w.right < 0 ? S : r0 + w.right + 1) - TK, w_pre = pre - TK;
-    const bool abs_ref = w.cap > 0.f && w.cap <= 64.f;
     float m = -INFINITY;   // reference maximum (log2 domain) of this group's last tile
     float l = 0.f;         // sum of this group's weights, relative to m
     int mine = 0, got = 0; // this group's tiles so far, references taken over from the other group
@@ -453,10 +453,12 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
       const bool whole = (j0 >= w_lo && j0 <= w_hi) || j0 <= w_pre;
       // First pass: the row's largest score, 32 columns at a time.  Scores that are masked, biased or under a cap without
       // coefficients go back to TMEM as they enter the exponent; the others are taken as they are in the second pass.
-      // Of capped scores the largest magnitude does: it bounds them, and as a reference it is at most 2^(2 cap log2 e tanh
-      // 3/4) above the largest weight (2^117 at cap 64, inside bf16's and fp32's range).
+      // Of capped scores the largest magnitude does: it bounds them and decides the polynomial's range.  As a reference it may
+      // be far above the largest score, where all are negative; eight columns bound that, and the largest itself is looked for
+      // where they are FAR or more below: the row's largest weight is 2^-FAR or more, so that neither lesser weights nor
+      // products with small values leave fp32's range.
       const bool ready = !whole || slope != 0.f || (w.cap > 0.f && !poly);
-      float mx = -INFINITY, mag = 0.f;
+      float mx = -INFINITY, mag = 0.f;   // under a cap: of the eight columns
 #pragma unroll
       for (int x = 0; x < TK; x += 32) {
         uint32_t v[32];
@@ -507,8 +509,10 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
           for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(sc[c]);
           tmem_st32(tm_s + x, v);
         }
-        if (!ready && w.cap > 0.f) mag = fmaxf(mag, magnitude(sc));
-        if (ready || !abs_ref) {
+        if (!ready && w.cap > 0.f) {
+          mag = fmaxf(mag, magnitude(sc));
+          mx = max3(max3(mx, sc[0], sc[8]), sc[16], sc[24]);
+        } else {
           float p0 = max3(sc[0], sc[1], sc[2]), p1 = max3(sc[3], sc[4], sc[5]);
 #pragma unroll
           for (int c = 6; c < 30; c += 4) {
@@ -518,17 +522,14 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
           mx = max3(mx, max3(p0, sc[30], sc[31]), p1);
         }
       }
-      const bool near = __all_sync(0xffffffffu, mag * inv_cap <= TANH_Y);   // capped scores in the polynomial's range
       bool placed = ready;   // the scores stand in TMEM as they enter the exponent
       if (!ready) {
         if (w.cap == 0.f) {
           mx *= f;
-        } else if (near) {
-          const float bound = abs_ref ? mag : mx;
-          mx = capped(make_float2(bound, bound), make_float2(0.f, 0.f)).x;
-        } else {   // a magnitude would be no reference for scores this far out
-          mx = cap_in_place(0, TK);
-          placed = true;
+        } else {
+          const float2 bound = capped(make_float2(mag, mx), make_float2(0.f, 0.f));
+          placed = !__all_sync(0xffffffffu, mag * inv_cap <= TANH_Y && bound.x - bound.y <= FAR);
+          mx = placed ? cap_in_place(0, TK) : bound.x;
         }
       }
       // the reference of the tile before: this group's own, or handed on by the other

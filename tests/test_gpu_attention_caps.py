@@ -74,3 +74,34 @@ def test_scores_around_the_end_of_the_polynomial(engines, dt, cap, view):  # noq
     q[:, :, 0] = torch.rand(n, H, generator=g, device="cuda") * 12 * cap ** 0.5
     k[:, :, 0] = (torch.rand(n, H, generator=g, device="cuda") * 2 - 1) * cap ** 0.5
     against_reference(engines, dt, q, k, v, [n], dict(view, cap=cap), D)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("cap", [20.0, 53.0, 60.0, 64.0])
+def test_scores_far_below_zero(engines, dt, cap):  # noqa: F811
+    """A tile of scores of -0.73 cap, then thousands further down: their small weights add up and are not lost."""
+    H, D, n = 1, 64, 4096
+    q, k, v = (torch.zeros(n, H, D, device="cuda", dtype=rows(0, 1, 1, D, dt).dtype) for _ in range(3))
+    q[:, :, 0] = 8.0
+    k[:64, :, 0], k[64:, :, 0] = -0.73 * cap, -cap
+    v[:64], v[64:] = 1.0, -1.0
+    against_reference(engines, dt, q, k, v, [n], dict(cap=cap), D)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("cap", [20.0, 50.0, 64.0, 300.0])
+@pytest.mark.parametrize("lift", [False, True])
+def test_small_values_under_scores_far_below_zero(engines, dt, cap, lift):  # noqa: F811
+    """Values of 1e-18 under scores of -0.7 cap (lift: but for one in each tile): their products with the weights stay in
+    range.  The results are rounded from 2^-100 and more: relative to them as ever."""
+    H, D, n = 2, 64, 256
+    q, k, v = (rows(260 + i, n, H, D, dt, 1e-2 if i < 2 else 1.0) for i in range(3))
+    q[:, :, 0] = 8.0
+    k[:, :, 0] = -0.7 * cap
+    if lift:
+        k[5::64, :, 0] = -0.6 * cap
+    out = run_packed(engines[dt], q, k, (v.float() * 1e-18).to(v.dtype), [n], dict(cap=cap), D)
+    b.sf_check(engines[dt])
+    v = np64((v.float() * 1e-18).to(v.dtype)) * 1e18
+    ref, spread, big = packed_reference(np64(q), np64(k), v, [n], dict(cap=cap), D, H)
+    check(np64(out) * 1e18, ref, spread, big, "packed", dt, D, cap, 0)
