@@ -508,8 +508,8 @@ typedef struct {
   int n_heads;      /* query heads                                                        */
   int n_kv_heads;   /* key/value heads; head h uses h / (n_heads / n_kv_heads)            */
   int head_dim;     /* 64 or 128                                                          */
-  float scale;      /* > 0                                                                */
-  float cap;        /* 0: no cap, else >= 1e-6                                            */
+  float scale;      /* > 0, a normal number, <= 1e30                                      */
+  float cap;        /* 0: no cap, else 1e-6 .. 1e30, and scale / cap a normal number      */
   int left, right;  /* positions seen before / after the query's own; -1: no limit
                        (left -1, right 0: causal)                                         */
 } sf_attn_params;

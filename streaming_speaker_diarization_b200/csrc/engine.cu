@@ -1405,8 +1405,11 @@ sf_status check_view(sf_engine* e, const sf_attn_params* p, const float* slopes,
   if (p->head_dim != 64 && p->head_dim != 128) return fail(e, SF_ESHAPE, "head_dim must be 64 or 128");
   if (p->n_kv_heads < 1 || p->n_heads < 1 || p->n_heads > 1024 || p->n_heads % p->n_kv_heads)
     return fail(e, SF_ESHAPE, "n_heads in [1, 1024], a multiple of n_kv_heads");
-  if (!(p->scale > 0.f) || !std::isfinite(p->scale) || !(p->cap == 0.f || p->cap >= 1e-6f) || !std::isfinite(p->cap) || p->left < -1 || p->right < -1)
-    return fail(e, SF_EINVAL, "attention parameters: finite scale > 0, cap 0 or finite and >= 1e-6, left and right >= -1");
+  // within these ends scale log2 e, scale / cap and cap log2 e are normal fp32 numbers
+  constexpr float LEAST = 1.17549435e-38f, MOST = 1e30f;
+  if (!(p->scale >= LEAST && p->scale <= MOST) || !(p->cap == 0.f || (p->cap >= 1e-6f && p->cap <= MOST && p->scale / p->cap >= LEAST)) ||
+      p->left < -1 || p->right < -1)
+    return fail(e, SF_EINVAL, "attention parameters: scale normal and <= 1e30, cap 0 or 1e-6 .. 1e30 and scale / cap normal, left and right >= -1");
   // positions stay below 2^30: a larger limit is none, and sums with it fit 32 bits
   *w = AttnView{p->scale, p->cap, std::min(p->left, 1 << 30), std::min(p->right, 1 << 30), slopes, prefix};
   return SF_OK;

@@ -2,8 +2,8 @@
 import numpy as np
 import pytest
 
-from test_gpu_attention_views import (b, cached_reference, check, dev, engines, make_cache, make_table, np64, rows, run_cached,  # noqa: F401
-                                      torch)
+from test_gpu_attention_views import (b, cached_reference, check, dev, engines, make_cache, make_table, np64,  # noqa: F401
+                                      packed_reference, rows, run_cached, run_packed, torch)
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,24 @@ def test_offsets_out_of_order_are_reported(engines, dt, cu):  # noqa: F811
             b.sf_check(eng)
         call(dev(sorted(cu)))
         b.sf_check(eng)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_scales_and_caps_at_the_ends_of_fp32(engines, dt):  # noqa: F811
+    """Scales and caps whose products leave fp32's normal range are refused; those just inside give finite results."""
+    eng, D, n = engines[dt], 64, 70
+    x, cu = rows(225, n, 2, D, dt), dev([0, n])
+    cache, held, table = make_cache(226, 5, 2, 16, D), dev([n]), dev([[0, 1, 2, 3, 4]])
+    for kw in (dict(scale=1e-39), dict(scale=2e30), dict(scale=-1.0), dict(cap=3e38), dict(cap=1.1e30), dict(cap=1e30, scale=1e-9),
+               dict(scale=float("nan")), dict(cap=float("inf"))):
+        p = b.attn_params(2, 2, D, **kw)
+        for call in (lambda: b.sf_attention_packed(eng, x, x, x, cu, torch.empty_like(x), p),
+                     lambda: b.sf_attention_cached(eng, x, cu, held, table, cache, torch.empty_like(x), p)):
+            with pytest.raises(b.SFError, match="SF_EINVAL"):
+                call()
+    for kw in (dict(scale=1.2e-38), dict(cap=1e30, scale=2e-8), dict(cap=1e30), dict(cap=1e-6, scale=1e30)):
+        p, out = b.attn_params(2, 2, D, **kw), [torch.empty_like(x) for _ in range(2)]
+        b.sf_attention_packed(eng, x, x, x, cu, out[0], p)
+        b.sf_attention_cached(eng, x, cu, held, table, cache, out[1], p)
+        assert all(torch.isfinite(o).all() for o in out)
+    b.sf_check(eng)
