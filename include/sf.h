@@ -584,7 +584,8 @@ SF_API sf_status sf_attention_cached(sf_engine* e, const void* d_q, int64_t ldq,
                                      const int* d_prefix, void* d_out, int64_t ldo, void* d_ws, uint64_t ws_bytes,
                                      void* cuda_stream);
 /* Bytes of workspace with which sf_attention_cached splits the keys of few,
- * long sequences over all SMs (0: none is used at these sizes). */
+ * long sequences over all SMs (0: none is used at these sizes).  max_len as
+ * for the call; 0: enough for a call with any max_len, 0 among them. */
 SF_API sf_status sf_attention_cached_workspace(sf_engine* e, int64_t T, int n, int max_len, const sf_attn_params* p,
                                                uint64_t* bytes);
 

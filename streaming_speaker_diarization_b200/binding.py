@@ -416,7 +416,7 @@ def kv_cache(k, v, k_scale, v_scale):
 
 
 def sf_attention_cached_workspace(eng, T, n, max_len, params):
-    """Bytes of workspace sf_attention_cached can use at these sizes."""
+    """Bytes of workspace sf_attention_cached can use at these sizes (max_len 0: at any length)."""
     size = ctypes.c_uint64()
     _check(lib.sf_attention_cached_workspace(eng, T, n, max_len, ctypes.byref(params), ctypes.byref(size)), eng)
     return size.value

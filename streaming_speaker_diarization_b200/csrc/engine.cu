@@ -18,6 +18,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <initializer_list>
 #include <memory>
@@ -1484,6 +1485,7 @@ sf_status sf_attention_cached_workspace(sf_engine* e, int64_t T, int n, int max_
   if (sf_status s = check_view(e, p, nullptr, nullptr, &w)) return s;
   if (T < 0 || T > MAX_ROWS || T * (p->n_heads / p->n_kv_heads) > MAX_ROWS || n < 1 || n > MAX_PACKED || max_len < 0)
     return fail(e, SF_ESHAPE, "rows, sequence count or max_len out of range");
+  if (max_len == 0) max_len = INT_MAX;   // the call takes its table's length then; longer ones never need less
   *bytes = T > 0 ? attention_cached_ws_bytes(e->cfg.precision == SF_FP32, T, n, p->n_heads, p->n_kv_heads, p->head_dim, max_len) : 0;
   return SF_OK;
 }

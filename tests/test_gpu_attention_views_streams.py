@@ -54,3 +54,28 @@ def test_a_block_just_freed_is_left_to_its_readers(long_request, handle):
     torch.cuda.synchronize()
     assert torch.equal(out, want[0]) and (y == 77).all()
     b.sf_check(eng)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,n,H,KV,D", [(1, 1, 8, 8, 64), (2, 1, 16, 2, 128), (3, 2, 4, 1, 128), (1, 1, 32, 1, 64), (40, 1, 4, 4, 64)])
+def test_a_workspace_for_any_length(engines, dt, T, n, H, KV, D):  # noqa: F811
+    """The size for max_len 0 is enough for a call with max_len 0, of whatever table, and for every other."""
+    eng, p = engines[dt], params(H, KV, D, {})
+    most = b.sf_attention_cached_workspace(eng, T, n, 0, p)
+    sizes = [b.sf_attention_cached_workspace(eng, T, n, x, p) for x in (1, 100, 4096, 8192, 10 ** 5, 10 ** 6, 2 ** 30)]
+    assert sizes == sorted(sizes) and sizes[-1] == most
+    if H * T <= 64:
+        assert most > 0
+    # the C call itself, with the documented 0 in both places
+    held = 9000
+    table, pages = make_table(205, [held] * n, 64)
+    cache, q = make_cache(206, pages, KV, 64, D), rows(207, T, H, D, dt)
+    new = [T // n + (i < T % n) for i in range(n)]
+    want = run_cached(eng, q, cache, table, [held] * n, new, {}, D)
+    cu = dev([sum(new[:i]) for i in range(n + 1)])
+    args = dev([held] * n), dev(table), torch.full_like(q, 7.0), torch.empty(max(most, 1), dtype=torch.uint8, device="cuda")
+    b._check(b.lib.sf_attention_cached(eng, q.data_ptr(), H * D, T, cu.data_ptr(), n, args[0].data_ptr(), args[1].data_ptr(),
+                                       table.shape[1], 0, cache.desc, p, None, None, args[2].data_ptr(), H * D,
+                                       args[3].data_ptr() if most else None, most, torch.cuda.current_stream().cuda_stream), eng)
+    b.sf_check(eng)
+    assert torch.equal(args[2], want)
