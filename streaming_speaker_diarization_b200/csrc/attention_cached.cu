@@ -713,7 +713,8 @@ __global__ void __launch_bounds__(256) attn_cached_merge_kernel(CachedArgs<E> a,
 
 namespace {
 int g_cached_sms = 148;
-int g_cached_clusters[2] = {48, 48};   // clusters of 8 CTAs resident at once, head dims 64 and 128
+// clusters of 8 CTAs resident at once: fp32 or not, head dim 128 or not, tiles of 16 rows or not
+int g_cached_clusters[2][2][2] = {{{48, 48}, {48, 48}}, {{48, 48}, {48, 48}}};
 
 // Rows of a tile, and how a call's keys are split: over clusters of nc CTAs
 // (joined on chip), and over ns clusters (joined by a second kernel) where
@@ -738,9 +739,9 @@ Plan cached_plan(bool f32, int64_t T, int n, int G, int n_kv, int D, int max_len
   // 235, 221, 227, 270)
   while (p.nc < 8 && ((units * p.nc * 2 <= slots && max_len >= p.nc * 128) || (units * p.nc < 2 * slots && max_len >= (int64_t)p.nc * 4096)))
     p.nc *= 2;
-  // more clusters than are resident at once would wait for a second round (one row over 180001 keys, 8 heads: 73 us with
-  // 6 clusters of 8 a head, 94 us with 9)
-  if (have_ws && p.nc == 8) p.ns = (int)std::min<int64_t>(g_cached_clusters[D == 128] / units, max_len / (8 * 512));
+  // more clusters than this kernel has resident at once would wait for a second round (180001 keys, 8 heads of 128: one row
+  // 73 us with 6 clusters of 8 a head, 94 us with 9; 13 rows, 3 CTAs an SM, 93 us with 6 and 124 us with 8)
+  if (have_ws && p.nc == 8) p.ns = (int)std::min<int64_t>(g_cached_clusters[f32][D == 128][p.R == 16] / units, max_len / (8 * 512));
   if (p.ns < 2) p.ns = 1;
   return p;
 }
@@ -795,7 +796,8 @@ template <typename E, int D> cudaError_t allow_smem() {
   }
   return cudaSuccess;
 }
-template <int D> cudaError_t resident_clusters(int* n) {
+// the lesser of both page forms
+template <typename E, int D, int NQ> cudaError_t resident_clusters() {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(8);
   cfg.blockDim = dim3(CW * 32);
@@ -806,7 +808,11 @@ template <int D> cudaError_t resident_clusters(int* n) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(n, attn_cached_kernel<bf16, D, 1, false>, &cfg);
+  int n = 0, n16 = 0;
+  cudaError_t r = cudaOccupancyMaxActiveClusters(&n, attn_cached_kernel<E, D, NQ, false>, &cfg);
+  if (r == cudaSuccess) r = cudaOccupancyMaxActiveClusters(&n16, attn_cached_kernel<E, D, NQ, true>, &cfg);
+  if (r == cudaSuccess) g_cached_clusters[sizeof(E) == 4][D == 128][NQ == 2] = std::min(n, n16);
+  return r;
 }
 }  // namespace
 
@@ -834,8 +840,13 @@ cudaError_t attention_cached_init_attributes() {
   if (r == cudaSuccess) r = allow_smem<float, 128>();
   if (r == cudaSuccess) r = allow_smem<bf16, 64>();
   if (r == cudaSuccess) r = allow_smem<bf16, 128>();
-  if (r == cudaSuccess) r = resident_clusters<64>(&g_cached_clusters[0]);
-  if (r == cudaSuccess) r = resident_clusters<128>(&g_cached_clusters[1]);
+  if (r == cudaSuccess) r = resident_clusters<bf16, 64, 1>();
+  if (r == cudaSuccess) r = resident_clusters<bf16, 64, 2>();
+  if (r == cudaSuccess) r = resident_clusters<bf16, 128, 1>();
+  if (r == cudaSuccess) r = resident_clusters<bf16, 128, 2>();
+  if (r == cudaSuccess) r = resident_clusters<float, 64, 1>();
+  if (r == cudaSuccess) r = resident_clusters<float, 64, 2>();
+  if (r == cudaSuccess) r = resident_clusters<float, 128, 1>();   // (its tiles have 8 rows at any size)
   return r;
 }
 

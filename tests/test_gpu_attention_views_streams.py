@@ -79,3 +79,15 @@ def test_a_workspace_for_any_length(engines, dt, T, n, H, KV, D):  # noqa: F811
                                        args[3].data_ptr() if most else None, most, torch.cuda.current_stream().cuda_stream), eng)
     b.sf_check(eng)
     assert torch.equal(args[2], want)
+
+
+@pytest.mark.parametrize("dt,D,rows_,tile,ctas", [("bf16", 64, 1, 8, 4), ("bf16", 64, 16, 16, 4), ("bf16", 128, 1, 8, 4),
+                                                  ("bf16", 128, 16, 16, 3), ("f32", 64, 1, 8, 4), ("f32", 64, 16, 16, 3),
+                                                  ("f32", 128, 1, 8, 3), ("f32", 128, 8, 8, 3)])
+def test_a_split_stays_within_what_is_resident(engines, dt, D, rows_, tile, ctas):  # noqa: F811
+    """One row tile over a very long past is split over as many clusters of 8 CTAs as its own kernel has resident at once
+    (ctas: CTAs of an SM by its registers): clusters that wait for a second round cost more than they bring."""
+    size = b.sf_attention_cached_workspace(engines[dt], 1, 1, 2 ** 30, b.attn_params(rows_, 1, D))
+    clusters = size / ((rows_ // tile + 1) * tile * (D + 2) * 4)
+    assert clusters == int(clusters)
+    assert 2 <= clusters <= torch.cuda.get_device_properties(0).multi_processor_count * ctas // 8
