@@ -533,8 +533,8 @@ SF_API sf_status sf_attention_packed(sf_engine* e, const void* d_q, int64_t ldq,
                                      const sf_attn_params* p, const float* d_slopes, const int* d_prefix, void* d_out,
                                      int64_t ldo, void* cuda_stream);
 
-/* A paged cache of keys and values in e4m3, one scale for each page and head
- * (value = code x scale); all memory is the caller's. */
+/* A paged cache of keys and values in e4m3, one scale >= 0 for each page and
+ * head (value = code x scale); all memory is the caller's. */
 typedef struct {
   void* d_k;           /* e4m3 [n_pages x n_kv_heads x page x head_dim] */
   void* d_v;
@@ -577,7 +577,10 @@ SF_API sf_status sf_kv_append(sf_engine* e, const void* d_k, int64_t ldk, const 
  *          these sizes (a smaller one is SF_ESHAPE), or NULL: fewer SMs share
  *          a long sequence then; calls that may run at once need one each
  * T x n_heads / n_kv_heads <= 2^26.  bf16 engines keep queries
- * exact and softmax weights to 11 bits, fp32 engines both to 22 bits. */
+ * exact and softmax weights to 11 bits, fp32 engines both to 22 bits.
+ * Value scales: the results are good to these bits where the scales of the
+ * pages that a row sees (0 counts as 2^-60) lie within a factor of 2^84; values
+ * under scales below 2^-60 are good to 2^-90. */
 SF_API sf_status sf_attention_cached(sf_engine* e, const void* d_q, int64_t ldq, int64_t T, const int* d_cu, int n,
                                      const int* d_held, const int* d_table, int table_cols, int max_len,
                                      const sf_kv_cache* cache, const sf_attn_params* p, const float* d_slopes,

@@ -24,6 +24,8 @@
 // V's page scale goes into the exponent: with s' = s + log2(vscale), the
 // weight 2^(s' - max s' + 14) lies in fp16's range whatever the scales are,
 // and the sum of weights takes weight / vscale, so nothing else is rounded.
+// Scales under 2^-60, 0 among them, count as 2^-60 there and take the rest in
+// the outputs' weights.
 //
 // One warp takes 32 keys a step and copies their rows whole with cp.async into
 // slots of its own, keys two steps ahead and values one.  A thread's fragment
@@ -48,7 +50,9 @@
 namespace sf {
 namespace {
 
-constexpr float VS_FLOOR = -80.f; // log2 of the smallest page scale told apart from 0
+// log2 of the least V scale that an exponent carries.  The weights' sum undoes the scale (2^60 at most), and a rescaling or
+// a weight of 2^-126 is the last one kept: scales 2^84 apart leave 2^-42 of the sum for a key, more than any count of keys
+constexpr float VS_FLOOR = -60.f;
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -413,18 +417,23 @@ __global__ void __launch_bounds__(CW * 32, cached_ctas(sizeof(E) == 4, D, NQ))
     const int ok = in.ok;
     const bool full = ok == 3 && j0 + 32 <= held && pos0 >= 0 &&
                       (((w.left < 0 || j0 >= pos1 - w.left) && (w.right < 0 || j0 + 31 <= pos0 + w.right)) || j0 + 32 <= pre);
-    float ks[2], lv[2], iv[2];
+    float ks[2], lv[2], iv[2], faint[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (h && !P16) {
         ks[1] = ks[0];
         lv[1] = lv[0];
         iv[1] = iv[0];
+        faint[1] = faint[0];
         break;
       }
       ks[h] = in.ks[h];
       lv[h] = lg2(in.vs[h]);
-      if (lv[h] < VS_FLOOR) lv[h] = VS_FLOOR;
+      faint[h] = 1.f;
+      if (lv[h] < VS_FLOOR) {   // the weights in the outputs alone are less by what the scale is under the floor
+        faint[h] = ex2(lv[h] - VS_FLOOR);
+        lv[h] = VS_FLOOR;
+      }
       iv[h] = lv[h] == lv[h] ? ex2(-lv[h]) : 1.f;   // NaN: the weight has it already
     }
     __syncwarp();   // every lane has read the slot
@@ -505,6 +514,7 @@ __global__ void __launch_bounds__(CW * 32, cached_ctas(sizeof(E) == 4, D, NQ))
           float2 p = __fadd2_rn(y[h][e], base);
           p = make_float2(ex2(p.x), ex2(p.y));
           sum[h] = e ? __fadd2_rn(sum[h], p) : p;
+          if (faint[h] != 1.f) p = make_float2(p.x * faint[h], p.y * faint[h]);
           uint32_t rest;
           pb[j][0][2 * h + e] = transpose8(half_pair(p.x, p.y, rest));
           if (F32) pb[j][NH - 1][2 * h + e] = transpose8(rest);

@@ -63,3 +63,24 @@ def test_scales_and_caps_at_the_ends_of_fp32(engines, dt):  # noqa: F811
         b.sf_attention_cached(eng, x, cu, held, table, cache, out[1], p)
         assert all(torch.isfinite(o).all() for o in out)
     b.sf_check(eng)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("scales", [(2.0 ** -70, 2.0 ** -70), (2.0 ** -75, 2.0 ** -62), (2.0 ** -62, 2.0 ** -75), (2.0 ** -90, 0.0),
+                                    (0.0, 0.0), (2.0 ** -100, 1.0), (1.0, 2.0 ** -100), (2.0 ** 24, 2.0 ** -100), (2.0 ** 24, 0.0),
+                                    (0.0, 2.0 ** 24), (2.0 ** 60, 2.0 ** -20), (2.0 ** 110, 2.0 ** 90)])
+def test_values_of_every_size(engines, dt, page, scales):  # noqa: F811
+    """Value scales far below and above 1.  Under 2^-60 the weights in the outputs carry the rest: they are off by half a step
+    of fp16's least, 2^-25, beside a largest weight of 2^14 or more, so by 2^-39 of 448 x 2^-60 for each key."""
+    H, KV, D, held = 4, 2, 64, 2 * page
+    cache, table = make_cache(227, 2, KV, page, D), np.array([[1, 0]])
+    cache.v_scale[1], cache.v_scale[0] = scales
+    q = rows(228, 9, H, D, dt)
+    out = np64(run_cached(engines[dt], q, cache, table, [held], [9], {}, D))
+    b.sf_check(engines[dt])
+    ref, spread, big = cached_reference(np64(q), cache, table, [held], [9], {}, D, H)
+    unit = max(max(scales), 2.0 ** -60)   # compared in units that the bound's own floor does not reach
+    low = held * 448 * 2.0 ** -39 * 2.0 ** -60 / unit
+    half = 2.0 ** -11 if dt == "bf16" else 2.0 ** -22
+    check(out / unit, ref / unit, spread / unit + low / half, big, "cached", dt, D, scales, 0)
