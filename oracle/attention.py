@@ -44,7 +44,7 @@ def viewed_attention(q, k, v, pos_q, scale, cap=0.0, left=-1, right=-1, prefix=0
         m = s.max(axis=1, keepdims=True, initial=-np.inf)
         p = np.exp(s - np.where(np.isfinite(m), m, 0.0))
         t = p.sum(axis=1, keepdims=True)
-        p = np.divide(p, t, out=np.zeros_like(p), where=t > 0)
+        p = np.divide(p, t, out=np.zeros_like(p), where=t != 0)   # (a NaN sum stays one)
         out[:, h], spread[:, h] = p @ vv, p @ np.abs(vv)
         big[:, h] = np.where(seen, scale * (np.abs(q[:, h]) @ np.abs(kk).T), 0.0).max(axis=1, initial=0.0)
     return out, spread, big
