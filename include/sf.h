@@ -494,8 +494,12 @@ SF_API sf_status sf_attention_mha(sf_engine* e, const void* d_qkv, const int* h_
  * Sequences are documents: no row sees another sequence's.  Elements of q, k,
  * v and out have the engine's precision (act); scores, softmax and sums are
  * fp32.  A NaN or infinity in a place that a row does not see does not reach
- * that row; one that it sees makes the row's results (of that dim, for a
- * value) a NaN or an infinity.
+ * that row.  Of what it sees, a NaN in the query or a key makes its results
+ * NaNs, and a value that is a NaN or infinite makes its results of that dim a
+ * NaN or an infinity.  Infinite queries and keys count by their scores: +inf
+ * makes the row NaN, -inf has weight 0 (zeros come out where all scores are
+ * -inf), and under a cap they are cap and -cap; sf_attention_cached makes a
+ * row NaN whose query is infinite.
  *
  * Offsets, lengths, tables and prefixes are device arrays that the call reads
  * when it runs: nothing is copied from the host and
