@@ -4,7 +4,8 @@ Every call below forwards to the C function of the same name.  Device
 buffers are torch CUDA tensors (their data pointers are passed), host arrays
 are numpy arrays, and `stream` defaults to torch's current CUDA stream.
 The library must have been built (``build.py``); importing this module on a
-machine without it raises immediately -- there is no fallback path.
+machine without it raises immediately -- there is no fallback path.  torch,
+and the native calls' module _calls.so, are loaded by what needs them first.
 """
 from __future__ import annotations
 
@@ -12,12 +13,6 @@ import ctypes
 import os
 
 import numpy as np
-import torch
-
-try:
-    from . import _calls
-except ImportError as e:
-    raise ImportError("_calls.so not built; run streaming_speaker_diarization_b200/build.py") from e
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libsf.so")
@@ -199,6 +194,7 @@ def sf_create(blob: bytes, cfg: sf_config):
     rc = lib.sf_create(ctypes.cast(buf, ctypes.c_void_p), len(blob), ctypes.byref(cfg), ctypes.byref(h))
     if rc != 0:
         raise SFError(f"sf_create: {STATUS.get(rc, rc)}")
+    import torch
     _engines[h.value] = (cfg.precision, torch.cuda.current_device())
     return h.value
 
@@ -425,6 +421,7 @@ def sf_attention_cached_workspace(eng, T, n, max_len, params):
 def _scratch(size, q, stream):
     """A workspace for one call on `stream` (None: torch's current one), from that stream's own pool: a block that
     torch takes on one stream may still be in use there, and only that stream's order keeps the two uses apart."""
+    import torch
     if stream is None:
         return torch.empty(size, dtype=torch.uint8, device=q.device)
     # 0 and 1 are CUDA's handles of the default stream
@@ -433,13 +430,30 @@ def _scratch(size, q, stream):
         return torch.empty(size, dtype=torch.uint8, device=q.device)
 
 
-# the calls of a single-frame step check and marshal their arguments natively (csrc/calls.cpp)
-_calls.setup(SFError, _engines, _check, torch._C._cuda_getCurrentRawStream, _scratch, sf_attn_params,
-             tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (lib.sf_attention_packed, lib.sf_kv_append, lib.sf_attention_cached,
-                                                                   lib.sf_attention_cached_workspace)))
-sf_attention_packed = _calls.sf_attention_packed
-sf_kv_append = _calls.sf_kv_append
-sf_attention_cached = _calls.sf_attention_cached
+# the calls of a single-frame step check and marshal their arguments natively (csrc/calls.cpp, which needs torch)
+_NATIVE = ("sf_attention_packed", "sf_kv_append", "sf_attention_cached")
+
+
+def _load_native():
+    path = os.path.join(HERE, "_calls.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} not built; run streaming_speaker_diarization_b200/build.py")
+    import torch
+    from . import _calls
+    _calls.setup(SFError, _engines, _check, torch._C._cuda_getCurrentRawStream, _scratch, sf_attn_params,
+                 tuple(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (*_NATIVE, "sf_attention_cached_workspace")))
+    globals().update({f: getattr(_calls, f) for f in _NATIVE})
+
+
+def __getattr__(name):
+    if name not in _NATIVE:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    _load_native()
+    return globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_NATIVE})
 
 
 def seg_params(**kw):
