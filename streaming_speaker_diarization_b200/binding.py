@@ -176,8 +176,40 @@ def _check(rc, eng=None):
         raise SFError(f"{STATUS.get(rc, rc)}: {msg}")
 
 
-# engine handle -> (precision, device index), for the native calls
+# engine handle -> (precision, device index), for the native calls: whoever creates or destroys one through `lib`
 _engines = {}
+
+
+def _current_device():
+    """Index of the device whose context is current, where an engine just made lives."""
+    dev = ctypes.c_int()
+    rc = ctypes.CDLL("libcuda.so.1").cuCtxGetDevice(ctypes.byref(dev))
+    if rc != 0:
+        raise SFError(f"SF_EDEVICE: no current device (CUDA driver error {rc})")
+    return dev.value
+
+
+def _created(rc, func, args):
+    if rc == 0:
+        out = getattr(args[-1], "_obj", args[-1])   # byref's, or a pointer, an array or the handle's place itself
+        out = out[0] if isinstance(out, (ctypes.Array, ctypes._Pointer)) else out
+        handle, cfg = getattr(out, "value", out), sf_config()
+        try:
+            _check(lib.sf_get_metadata(handle, ctypes.byref(cfg)))
+            _engines[handle] = (cfg.precision, _current_device())
+        except BaseException:
+            lib.sf_destroy(handle)
+            raise
+    return rc
+
+
+def _destroyed(rc, func, args):
+    _engines.pop(getattr(args[0], "value", args[0]), None)
+    return rc
+
+
+lib.sf_create.errcheck = lib.sf_create_from_file.errcheck = _created
+lib.sf_destroy.errcheck = _destroyed
 
 
 def default_config(**kw):
@@ -194,13 +226,10 @@ def sf_create(blob: bytes, cfg: sf_config):
     rc = lib.sf_create(ctypes.cast(buf, ctypes.c_void_p), len(blob), ctypes.byref(cfg), ctypes.byref(h))
     if rc != 0:
         raise SFError(f"sf_create: {STATUS.get(rc, rc)}")
-    import torch
-    _engines[h.value] = (cfg.precision, torch.cuda.current_device())
     return h.value
 
 
 def sf_destroy(eng):
-    _engines.pop(eng, None)
     _check(lib.sf_destroy(eng))
 
 

@@ -20,7 +20,7 @@ struct {
   decltype(&sf_kv_append) append;
   decltype(&sf_attention_cached) cached;
   decltype(&sf_attention_cached_workspace) workspace;
-  PyObject *error, *engines, *check, *raw_stream, *scratch, *params, *desc, *device;
+  PyObject *error, *engines, *check, *raw_stream, *scratch, *params, *desc, *device, *value;
 } g;
 
 struct Failed {};   // a Python error is set
@@ -74,19 +74,27 @@ int64_t length(PyObject* o, const char* name) {
   return t.size(0);
 }
 
+struct Ref {   // owned
+  PyObject* o;
+  explicit Ref(PyObject* x) : o(x) {}
+  Ref(const Ref&) = delete;
+  ~Ref() { Py_XDECREF(o); }
+};
+
 struct Engine {
-  PyObject* key;
+  Ref key;   // the handle as an int
   sf_engine* e;
   at::ScalarType act;
   int device;
 
-  explicit Engine(PyObject* eng) : key(eng) {
-    PyObject* known = PyDict_GetItemWithError(g.engines, eng);
+  // eng: an int, or the ctypes pointer that holds it
+  explicit Engine(PyObject* eng) : key(PyLong_Check(eng) ? Py_NewRef(eng) : PyObject_GetAttr(eng, g.value)) {
+    PyObject* known = key.o ? PyDict_GetItemWithError(g.engines, key.o) : nullptr;
     if (!known) {
       if (PyErr_Occurred()) PyErr_Clear();
       fail("SF_EINVAL: not an engine of sf_create");
     }
-    e = static_cast<sf_engine*>(PyLong_AsVoidPtr(eng));
+    e = static_cast<sf_engine*>(PyLong_AsVoidPtr(key.o));
     act = PyObject_IsTrue(PyTuple_GET_ITEM(known, 0)) ? at::kBFloat16 : at::kFloat;
     device = (int)PyLong_AsLong(PyTuple_GET_ITEM(known, 1));
     if (PyErr_Occurred()) throw Failed();
@@ -134,7 +142,7 @@ struct Engine {
   }
   void done(sf_status rc) const {
     if (rc == SF_OK) return;
-    PyObject* r = PyObject_CallFunction(g.check, "iO", (int)rc, key);
+    PyObject* r = PyObject_CallFunction(g.check, "iO", (int)rc, key.o);
     Py_XDECREF(r);
     throw Failed();
   }
@@ -292,6 +300,7 @@ PyObject* setup(PyObject*, PyObject* args) {
   g.workspace = reinterpret_cast<decltype(g.workspace)>(f[3]);
   g.desc = PyUnicode_InternFromString("desc");
   g.device = PyUnicode_InternFromString("device");
+  g.value = PyUnicode_InternFromString("value");
   Py_RETURN_NONE;
 }
 
