@@ -6,6 +6,7 @@ import subprocess
 import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
+from importlib import metadata
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -55,9 +56,14 @@ def build(verbose: bool = False) -> str:
 
 
 def _build_calls():
-    """_calls.so, csrc/calls.cpp: a Python module that takes torch tensors and calls libsf.so's functions."""
+    """_calls.so, csrc/calls.cpp: a Python module that takes torch tensors and calls libsf.so's functions; for one torch
+    and one Python, whose versions stand in a file beside the objects."""
     src, header = os.path.join(CSRC, "calls.cpp"), os.path.join(ROOT, "include", "sf.h")
-    if os.path.exists(CALLS) and os.path.getmtime(CALLS) >= max(os.path.getmtime(f) for f in (src, header)):
+    stamp = os.path.join(BUILD, "calls.versions")
+    versions = f"torch {metadata.version('torch')}, Python {sys.version}\n"
+    built_for = open(stamp).read() if os.path.exists(stamp) else None
+    if built_for == versions and os.path.exists(CALLS) and \
+            os.path.getmtime(CALLS) >= max(os.path.getmtime(f) for f in (src, header)):
         return
     import torch
     base = os.path.dirname(torch.__file__)
@@ -69,6 +75,8 @@ def _build_calls():
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    with open(stamp, "w") as f:
+        f.write(versions)
 
 
 if __name__ == "__main__":
