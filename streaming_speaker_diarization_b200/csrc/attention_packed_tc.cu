@@ -195,26 +195,18 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
   uint64_t* pv_done = p_full + NG;                                  // P V added to O
   uint64_t* o_done = pv_done + 1;                                   // all products done
   uint64_t* handed = o_done + 1;                                    // [2][4] a warp's rows' references handed on
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(handed + 8);
+  uint64_t* v_tail = handed + 8;                                    // values that reach behind the sequence have landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_tail + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   // warp-uniform values, and known to be: the MMA warp computes with them in uniform registers
   auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (threadIdx.x == 64) {
-    for (int b = 0; b < L::NS; ++b) {
-      mbar_init(&full[b], 1);
-      mbar_init(&empty[b], 1);
-    }
-    mbar_init(q_full, 1);
-    for (int g = 0; g < NG; ++g) {
-      mbar_init(&s_full[g], 1);
-      mbar_init(&p_full[g], 4);
-    }
-    mbar_init(pv_done, 1);
-    mbar_init(o_done, 1);
-    for (int k = 0; k < 8; ++k) mbar_init(&handed[k], 1);
-    *abort_flag = 0;
+  if (warp == 2) {   // a lane each: one thread after the other they delayed every CTA
+    constexpr int first_p = 2 * L::NS + 1 + NG, count = first_p + NG + 2 + 8 + 1;
+    static_assert(count <= 32, "a lane per barrier");
+    if (lane < count) mbar_init(&full[lane], lane >= first_p && lane < first_p + NG ? 4 : 1);
+    if (lane == 0) *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -272,6 +264,8 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
   };
 
   if (warp < 4) {
+    // the copy of the last values, where they reach behind the sequence (else none)
+    const int v_rows = S - tile_of(nt - 1) * TK, tail = v_rows < TK ? 2 * nt - 1 : -1;
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::REG_LOW));
     if (warp == 0 && nt > 0) {
       // -------------------------------------------------------------- loads
@@ -296,9 +290,10 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
           }
           bool is_v;
           const int t = copy_tile(c, is_v);
-          mbar_expect_tx(&full[b], L::TILE);
+          uint64_t* bar = c == tail ? v_tail : &full[b];
+          mbar_expect_tx(bar, L::TILE);
           for (int x = 0; x < D / 64; ++x)
-            tma_load_2d(sRing + b * L::TILE + x * TK * 128, is_v ? &t_v : &t_k, &full[b], kvh * D + 64 * x, sb + tile_of(t) * TK);
+            tma_load_2d(sRing + b * L::TILE + x * TK * 128, is_v ? &t_v : &t_k, bar, kvh * D + 64 * x, sb + tile_of(t) * TK);
         }
         if (*abort_flag) {   // let this CTA's own loads land before its shared memory is released
           auto drain = [&](uint64_t* bar, uint32_t parity) {
@@ -307,7 +302,8 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
             }
           };
           drain(q_full, 0);
-          for (int k = c - L::NS > 0 ? c - L::NS : 0; k < c; ++k) drain(&full[k % L::NS], (k / L::NS) & 1);
+          for (int k = c - L::NS > 0 ? c - L::NS : 0; k < c; ++k)
+            drain(k == tail ? v_tail : &full[k % L::NS], k == tail ? 0 : (k / L::NS) & 1);
         }
       }
       __syncwarp();
@@ -369,6 +365,20 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
       if (!ok) *abort_flag = 1;
       __syncwarp();
       pdl_trigger();
+    } else if (warp == 3 && tail > 0) {
+      // ------------------------------------------------ rows behind the sequence
+      // The last values may reach behind it: those rows are made zeros before the products see them, since a NaN there would
+      // have every row computed again (1125 rows: 6500 us against 25)
+      if (__all_sync(0xffffffffu, mbar_wait(v_tail, 0, abort_flag))) {
+        uint8_t* tile_v = sRing + tail % L::NS * L::TILE;
+#pragma unroll 1
+        for (int b = v_rows * 128 + 16 * lane; b < TK * 128; b += 512)
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x) *reinterpret_cast<uint4*>(tile_v + x * TK * 128 + b) = make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[tail % L::NS]);
+      }
     }
     if (nc > 1) {
       if (warp == 1) {

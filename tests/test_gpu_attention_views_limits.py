@@ -84,3 +84,27 @@ def test_values_of_every_size(engines, dt, page, scales):  # noqa: F811
     low = held * 448 * 2.0 ** -39 * 2.0 ** -60 / unit
     half = 2.0 ** -11 if dt == "bf16" else 2.0 ** -22
     check(out / unit, ref / unit, spread / unit + low / half, big, "cached", dt, D, scales, 0)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,H", [([1], 2), ([63], 2), ([200, 321], 8), ([1500], 2), ([2309], 2), ([322] * 40, 16)])
+@pytest.mark.parametrize("view", [{}, dict(right=0), dict(left=60, right=3, prefix=[130] * 40)])
+def test_what_lies_behind_a_sequence_changes_no_bit(engines, dt, D, lens, H, view):  # noqa: F811
+    """Keys and values behind the last sequence, and a sequence's neighbour's, that are not finite: the results of zeros there,
+    to the bit (a row computed again from its own keys alone would differ in its roundings, and cost a hundred times as much)."""
+    T = sum(lens)
+    q, k, v = (rows(290 + i, T + 70, H, D, dt) for i in range(3))
+    outs = []
+    for x in (0.0, float("nan"), float("inf")):
+        for t in (k, v):
+            t[T:] = x
+        if len(lens) > 2:
+            for t in (k, v):
+                t[lens[0]:2 * lens[0]] = x   # the second sequence
+        outs.append(run_packed(engines[dt], q, k, v, lens, view, D))
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    if len(lens) > 2:
+        keep[lens[0]:2 * lens[0]] = False
+    assert all(torch.equal(o[:T][keep], outs[0][:T][keep]) for o in outs[1:]) and torch.isfinite(outs[0][:T]).all()
+    b.sf_check(engines[dt])
