@@ -499,7 +499,8 @@ SF_API sf_status sf_attention_mha(sf_engine* e, const void* d_qkv, const int* h_
  * NaN or an infinity.  Infinite queries and keys count by their scores: +inf
  * makes the row NaN, -inf has weight 0 (zeros come out where all scores are
  * -inf), and under a cap they are cap and -cap; sf_attention_cached makes a
- * row NaN whose query is infinite.
+ * row NaN whose query is infinite, and may make one NaN in all dims for a NaN
+ * code of one value.
  *
  * Offsets, lengths, tables and prefixes are device arrays that the call reads
  * when it runs: nothing is copied from the host and
@@ -560,8 +561,8 @@ typedef struct {
  * |x| / 448); where it grows, the older rows' codes are rounded again to the
  * new scale.  Rows behind d_held in a page keep their bytes.  A NaN or
  * infinity makes its page's scale NaN or infinite for that head (its new codes
- * are 0), and a row that sees the page a NaN.  A page that
- * two sequences of one call would write has undefined contents. */
+ * are 0), and a row that sees the page a NaN.  A page that one call would
+ * write at two places of its table has undefined contents. */
 SF_API sf_status sf_kv_append(sf_engine* e, const void* d_k, int64_t ldk, const void* d_v, int64_t ldv, int64_t T,
                               const int* d_cu, int n, const int* d_held, const int* d_table, int table_cols,
                               const sf_kv_cache* cache, void* cuda_stream);

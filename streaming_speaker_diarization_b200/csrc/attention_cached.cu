@@ -87,6 +87,12 @@ __device__ __forceinline__ uint32_t half_pair(float x0, float x1, uint32_t& rest
   rest = h2_bits(__floats2half2_rn(x0 - b.x, x1 - b.y));
   return h2_bits(h);
 }
+// zeros in the place of NaN codes; whether there was one
+__device__ __forceinline__ uint32_t clear_nan(uint32_t& w) {
+  const uint32_t is = __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+  w &= ~is;
+  return is;
+}
 // transpose of an 8 x 8 matrix of 16-bit elements held as mma fragments
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
@@ -415,8 +421,10 @@ __global__ void __launch_bounds__(CW * 32, cached_ctas(sizeof(E) == 4, D, NQ))
     }
     // ---- weights
     const int ok = in.ok;
-    const bool full = ok == 3 && j0 + 32 <= held && pos0 >= 0 &&
-                      (((w.left < 0 || j0 >= pos1 - w.left) && (w.right < 0 || j0 + 31 <= pos0 + w.right)) || j0 + 32 <= pre);
+    // every row sees every key that is there; and all 32 are
+    const int j1 = min(j0 + 32, held);
+    const bool all_see = pos0 >= 0 && (((w.left < 0 || j0 >= pos1 - w.left) && (w.right < 0 || j1 - 1 <= pos0 + w.right)) || j1 <= pre);
+    const bool full = all_see && ok == 3 && j0 + 32 <= held;
     float ks[2], lv[2], iv[2], faint[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -529,6 +537,26 @@ __global__ void __launch_bounds__(CW * 32, cached_ctas(sizeof(E) == 4, D, NQ))
     if (!full) {   // places without a row hold whatever was there: no NaN code may meet a zero weight
       for (int r = copy_row; r < 32; r += RPC)
         if (j0 + r >= held || !(ok >> (r >> 4) & 1)) *reinterpret_cast<uint4*>(slot.v + piece_at<D>(r, copy_piece)) = make_uint4(0, 0, 0, 0);
+      __syncwarp();
+    }
+    if (!all_see) {   // nor may one of a row that is there: the rows that see it get their NaN here
+      uint32_t lost = 0;   // keys with a NaN among their values
+      for (int r = copy_row; r < 32; r += RPC) {
+        uint4* at = reinterpret_cast<uint4*>(slot.v + piece_at<D>(r, copy_piece));
+        uint4 x = *at;
+        if (clear_nan(x.x) | clear_nan(x.y) | clear_nan(x.z) | clear_nan(x.w)) {
+          lost |= 1u << r;
+          *at = x;
+        }
+      }
+      for (lost = __reduce_or_sync(0xffffffffu, lost); lost; lost &= lost - 1) {
+        const int key = j0 + __ffs(lost) - 1;
+#pragma unroll
+        for (int j = 0; j < NQ; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (seen(key, pos[j][i])) l[j][i] = NAN;
+      }
       __syncwarp();
     }
     // ---- output: rows g, g + 8 of dim tile d are this lane's dims 2 d, 2 d + 1; slots 2 t, 2 t + 1 of 8 keys its rows

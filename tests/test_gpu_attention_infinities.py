@@ -71,3 +71,37 @@ def test_cached_query(engines, dt, cap, D):  # noqa: F811
     ref, spread, big = cached_reference(np64(fine), cache, table, [held], [new], dict(cap=cap, right=0), D, H)
     out[lost], ref[lost] = 0.0, 0.0
     check(out, ref, spread, big, "cached", dt, D, cap, 0)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D,page", [(64, 16), (64, 64), (128, 16), (128, 32)])
+@pytest.mark.parametrize("view", [dict(right=0), dict(left=40, right=0), dict(left=9, right=5, prefix=[20]), {}])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_cached_nan_codes(engines, dt, D, page, view, which):  # noqa: F811
+    """NaN codes among a sequence's cached rows (a caller's: sf_kv_append writes none): the rows that see them are NaN in that
+    head, at least in that dim of a value; the others are what they are without them."""
+    H, KV, held, new = 4, 2, 150, 23
+    table, pages = make_table(288, [held], page)
+    cache = make_cache(289, pages, KV, page, D)
+    q = rows(290, new, H, D, dt)
+    spots = [(5, 0, 3), (70, 1, 60), (131, 0, 17), (140, 0, 18), (149, 1, 40)]
+    codes = getattr(cache, which).view(torch.uint8)
+    for j, g, d in spots:
+        codes[table[0, j // page], g, j % page, d] = 0
+    ref, spread, big = cached_reference(np64(q), cache, table, [held], [new], view, D, H)
+    for n, (j, g, d) in enumerate(spots):
+        codes[table[0, j // page], g, j % page, d] = 0x7f if n % 2 else 0xff
+    out = np64(run_cached(engines[dt], q, cache, table, [held], [new], view, D))
+    b.sf_check(engines[dt])
+    i = np.arange(held - new, held)
+    pre, left, right = view.get("prefix", [0])[0], view.get("left", -1), view.get("right", -1)
+    lost = np.zeros((new, H), bool)
+    for j, g, d in spots:
+        sees = (j < pre) | (((left < 0) | (i - j <= left)) & ((right < 0) | (j - i <= right)))
+        lost[np.ix_(sees, range(2 * g, 2 * g + 2))] = True
+        assert np.isnan(out[sees][:, 2 * g:2 * g + 2, d] if which == "v" else out[sees][:, 2 * g:2 * g + 2]).all()
+    assert np.isfinite(out[~lost]).all()
+    if view.get("left", -1) >= 0:
+        assert lost.any() and not lost.all()
+    out[lost], ref[lost] = 0.0, 0.0
+    check(out, ref, spread, big, "cached", dt, D, view, 0)
