@@ -3,10 +3,11 @@
 // the score and mask).  Row r of the call's rows of a sequence with `held`
 // cached rows stands at position held - n + r.
 //
-// The codes of a sequence are read once for all query rows of a key/value
-// head: the G heads that share it times the new rows are packed as rows of 8-
-// or 16-row tiles (the 128-row tiles of the tcgen05 products would be nearly
-// empty, and the bytes of the codes, not the products, bound the work).
+// The codes of a sequence are read once for up to 16 query rows of a key/value
+// head (8 in fp32 at heads of 128): the G heads that share it times the new rows
+// are packed as rows of 8- or 16-row tiles, each of which reads them (the 128-row
+// tiles of the tcgen05 products would be nearly empty for the few rows of a
+// step, whose work the bytes of the codes bound, not the products).
 //
 // Products are mma.sync m16n8k16 with fp16 operands and fp32 sums, keys (and
 // then output dims) along M, query rows along N, so a tile of up to 8 rows
@@ -20,7 +21,8 @@
 // a bias: fp32 outputs are summed over 16 keys there and rounded onwards, the
 // second parts' scores in a chain of their own (7 rows over 1740 keys,
 // relative error 1.1e-6 -> 4.8e-7; the formula in fp32 operations 5.1e-7; 16
-// requests of 3 rows over up to 6000 keys 23.7 -> 25.9 us).
+// requests of 3 rows over up to 6000 keys 23.7 -> 25.9 us).  (What is said of
+// NaN codes and tiny scales below added about 2 % to 16 x 3 and 64 x 13 rows.)
 // V's page scale goes into the exponent: with s' = s + log2(vscale), the
 // weight 2^(s' - max s' + 14) lies in fp16's range whatever the scales are,
 // and the sum of weights takes weight / vscale, so nothing else is rounded.

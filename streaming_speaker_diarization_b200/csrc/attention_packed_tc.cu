@@ -33,14 +33,17 @@
 // for a warp's rows: tanh(y) / y as a polynomial of degree 4 in y^2 (our own
 // fit at Chebyshev nodes, relative error 5.9e-7 on [0, 3/4]), with the score
 // factor, the cap and log2 e in its coefficients, so that the exponent is one
-// more multiply-add; beyond, and for caps whose coefficients leave fp32's range, the polynomial or, for scores beyond its range,
-// 1 - 2 / (2^(2 y log2 e) + 1), whose absolute error of 2.5e-7 is small against
-// a score of that size.
+// more multiply-add.  Other tiles, and caps whose coefficients leave fp32's
+// range, have their scores rewritten in TMEM: by the polynomial in s / cap
+// where that is in its range, else by 1 - 2 / (2^(2 y log2 e) + 1), whose
+// absolute error of 2.5e-7 is small against a score of that size.
 //
 // 0 x V of rows that do not see a key of their tile would carry an infinity or
 // NaN over: a row whose result is not finite although its sum is, and that sees
-// no such value, is computed again from its own keys (attn_packed_row.cuh).  Every wait is bounded: a wait that runs out
-// raises ERR_TIMEOUT, the CTA drains its own copies and frees its TMEM.
+// no such value, is computed again from its own keys (attn_packed_row.cuh).
+// Rows of the last value tile that lie behind the sequence are cleared by warp 3
+// first.  Every wait is bounded: a wait that runs out raises ERR_TIMEOUT, the CTA
+// drains its own copies and frees its TMEM.
 #include "attn_common.cuh"
 #include "attn_packed_row.cuh"
 #include "attn_view.cuh"
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(PTc<NG, D>::THREADS, PTc<NG, D>::PER_SM)
   const unsigned unit = blockIdx.x >> nc_log2, behind = unit / (unsigned)a.n_heads;   // slots behind this one in the list
   const int h = unit - behind * a.n_heads;
   const int kvh = (unsigned)h / (unsigned)G;
-  // one warp looks the tile up (64 windows: 31.5 us, all eight 34.7) while another takes TMEM
+  // one warp looks the tile up (64 windows, measured when added: 31.5 us, all eight 34.7) while another takes TMEM
   __shared__ int found[4];
   if (warp == 0) {
     int tile, sb, se;

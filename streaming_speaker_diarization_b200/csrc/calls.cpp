@@ -318,7 +318,8 @@ PyMethodDef methods[] = {
     {"sf_attention_cached", CALL(cached),
      "sf_attention_cached(eng, q, cu, held, table, cache, out, params, slopes=None, prefix=None, max_len=0, stream=None)\n--\n\n"
      "q, out: act [T, n_heads, head_dim], the sequences' newest rows; cu, held, table, cache as for sf_kv_append.\n"
-     "Few, long sequences take a workspace from torch's allocator."},
+     "Few, long sequences take a workspace from torch's allocator, on the call's stream (captured by torch.cuda.graph,\n"
+     "whose pool keeps it)."},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
