@@ -583,9 +583,10 @@ SF_API sf_status sf_kv_append(sf_engine* e, const void* d_k, int64_t ldk, const 
  *          a long sequence then; calls that may run at once need one each
  * T x n_heads / n_kv_heads <= 2^26.  bf16 engines keep queries
  * exact and softmax weights to 11 bits, fp32 engines both to 22 bits.
- * Value scales: the results are good to these bits where the scales of the
- * pages that a row sees (0 counts as 2^-60) lie within a factor of 2^84; values
- * under scales below 2^-60 are good to 2^-90. */
+ * Value scales: weights are kept to these bits down to 2^-28 of the largest
+ * weight x scale and to 2^-39 of it below (of values under scales below 2^-60: of
+ * 2^-60 at least), where the scales of the pages that a row sees (0 counts as
+ * 2^-60) lie within a factor of 2^84. */
 SF_API sf_status sf_attention_cached(sf_engine* e, const void* d_q, int64_t ldq, int64_t T, const int* d_cu, int n,
                                      const int* d_held, const int* d_table, int table_cols, int max_len,
                                      const sf_kv_cache* cache, const sf_attn_params* p, const float* d_slopes,
